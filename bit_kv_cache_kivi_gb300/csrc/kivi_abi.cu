@@ -689,15 +689,17 @@ int evict_step(const kivi_cache* c) { return ring_slots(c->cfg) / c->cfg.group; 
 
 // ---- attention over blocks: splits and workspace ----
 
-// Splits of a (batch, kv-head, head chunk) at most.
+// Splits of a (batch, kv-head, head chunk) at most; never fewer than the
+// longest tail's and a packed one beside it.
 int block_max_splits(const kivi_config& c) {
   const long u = attention_units(c);
   const int nb = kivi::attn_key_blocks(c.n_q_heads / c.n_kv_heads);
   long s = 3l * kivi::attn_ctas_per_sm(c.bits, nb) * kivi::kTargetSMs / u;
   const long by_len = max_tail_splits(c) + (c.max_tokens + 31) / 32;
   if (s > by_len) s = by_len;
+  if (s > kivi::kMaxSplits) s = kivi::kMaxSplits;
   if (s < max_tail_splits(c) + 1) s = max_tail_splits(c) + 1;
-  return (int)(s < kivi::kMaxSplits ? s : kivi::kMaxSplits);
+  return (int)s;
 }
 
 kivi::SplitCfg block_split_cfg(const kivi_cache* c) {
@@ -725,6 +727,8 @@ kivi_status attention_checks(kivi_cache* c, const void* q, kivi_dtype q_dtype, c
   if (!c) return KIVI_EINVAL;
   if (!dtype_ok(q_dtype)) return KIVI_EDTYPE;
   if (!q || !out) return KIVI_EINVAL;
+  // two levels of merges: kFlatMerge groups of kMergeGroup splits
+  if (max_tail_splits(c->cfg) + 1 > kivi::kFlatMerge * kivi::kMergeGroup) return KIVI_ESHAPE;
   for (int b = 0; b < (c->uniform ? 1 : c->cfg.batch); ++b)
     if (len_of(c, b) <= 0) return KIVI_ESTATE;
   if (!workspace || !aligned16(workspace) || ws_bytes < kivi_block_workspace_bytes(c)) return KIVI_EWORKSPACE;

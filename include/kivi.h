@@ -409,7 +409,8 @@ kivi_status kivi_select_blocks(kivi_cache *c, const float *scores, int n_blocks,
  * kivi_set_attention_splits applies.  The softmax weights enter the value
  * product as fp16 pairs (one fp16 each for bf16 queries, whose outputs round
  * at 2^-9, and in kivi_decode_attention), so f32 queries get outputs close to
- * f32.  KIVI_ESHAPE when n_list is negative. */
+ * f32.  KIVI_ESHAPE when n_list is negative, and, as from the attention calls
+ * below, when R is above 65440. */
 kivi_status kivi_decode_attention_blocks(kivi_cache *c, const void *q,
                                          kivi_dtype q_dtype, const int *blocks,
                                          int n_list, void *out,

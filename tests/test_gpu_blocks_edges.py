@@ -1,0 +1,39 @@
+"""Block operators where their documentation allows more than an ordinary
+cache asks for, each against its formula in 64 bits."""
+import numpy as np
+import pytest
+import torch
+
+import kivi_testlib as T
+from test_gpu_blocks import G, Pair, _lib, err, random_list  # noqa: F401  (_lib builds the library)
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("R,policy,grp,bits,tiles", [(16384, 0, 4, 2, 700), (16384, 1, 7, 4, 37), (16320, 0, 1, 8, 64),
+                                                     (20480, 0, 4, 2, 300), (65440, 0, 2, 2, 20)])
+def test_long_windows(R, policy, grp, bits, tiles):
+    """The longest tail a window leaves, R + 31 tokens of which 31 values are packed already (or, shared, of whose next
+    group 31 tokens are there): more than 256 splits of 64 tokens, and the packed ones beside them."""
+    l = R + 31 + G * tiles
+    p = Pair(B=2, H=2, T_=l, R=R, policy=policy, grp=grp, bits=bits, lengths=[l, 100], seed=2, capacity=-(-l // R) * R)
+    assert p.blocks(0) == tiles
+    rng = np.random.default_rng(1)
+    lists = np.stack([[random_list(rng, p.blocks(b), 20, "some") for _ in range(2)] for b in range(2)])
+    dev, every = torch.from_numpy(lists).cuda(), torch.zeros((2, 2, -(-l // G)), device="cuda")
+    for splits in (0, 400):
+        p.cache.set_splits(splits)
+        every.zero_()
+        out = T.out_float(p.cache.attention_blocks(p.q, dev)).reshape(2, 2, grp, 128)
+        whole = T.out_float(p.cache.attention_mass(p.q, every)).reshape(2, 2, grp, 128)
+        mass = every.cpu().numpy()
+        for b in range(2):
+            for h in range(2):
+                row = lists[b, h][lists[b, h] >= 0].astype(np.int64)
+                tokens = np.concatenate([(row[:, None] * G + np.arange(G)).reshape(-1), np.arange(p.blocks(b) * G, p.lengths[b])])
+                assert err(out[b, h], p.attend(b, h, tokens)[1], "f16") <= T.ATTN_TOL, (splits, b, h)
+                w, ref = p.attend(b, h, np.arange(p.lengths[b]))
+                assert err(whole[b, h], ref, "f16") <= T.ATTN_TOL, (splits, b, h)
+                per = np.zeros(mass.shape[2])
+                np.add.at(per, np.arange(p.lengths[b]) // G, w.sum(0))
+                assert np.allclose(mass[b, h], per, rtol=1e-4, atol=1e-6)  # (bounds: test_attention_mass)

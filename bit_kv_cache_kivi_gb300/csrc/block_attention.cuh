@@ -581,7 +581,6 @@ __device__ __forceinline__ void packed_blocks_split(const CacheView& cv, const A
   make_q_tables<BITS, NB, MODE>(sv, a, q4, cv.n_out > 0);
   if (wait_late) {
     grid_dependency_wait();
-    if (!a.next_late) grid_launch_dependents();
     id = my_entry(0);
     begin();
   }
@@ -785,10 +784,9 @@ __device__ __forceinline__ void merge_splits(const float* po, const float* pml, 
 // ones (window_last): grid (H * head_chunks, B, splits).  128 units of 128 8-bit
 // tiles (384 CTAs for 304 places) take 32.5 us so, 37.6 unit by unit; 8 units of
 // 256 tiles 10.0 us so, 9.7 unit by unit.
-// The next launch may start (next_late) at once where a second one finds places
-// too, else once a CTA has its partial: CTAs that only wait would take the places
-// unevenly, and with them the next launch's balance (8 units of 256 tiles, 144
-// CTAs: 9.7 us at once, 10.9 late; 384 units of 64 tiles: 36.3 and 33.9).
+// The next launch starts when this one has completed (attention calls with the
+// overlap on read its output without waiting), but for the weights' launch of
+// the same call (mass_kernel).
 template <int BITS, int NB, int MODE>
 __global__ void __launch_bounds__(128, attn_ctas_per_sm(BITS, NB))
     block_attn_kernel(CacheView cv, AttnArgs a, const SeqLens lens) {
@@ -813,14 +811,14 @@ __global__ void __launch_bounds__(128, attn_ctas_per_sm(BITS, NB))
                         : make_plan(lens.l[b], cv.R, cv.policy, a.scfg, attn_listed(MODE) ? a.list_len : -1);
   const int zt = a.window_last ? z + p.tail_splits : z;
   const int s = zt < p.splits ? zt : zt - p.splits;
-  // Every launch starts while the one before it ends, waits for it before it
-  // touches memory, and then lets the next one start.  kPdlAll (its list comes
-  // from the launch before it, its q and cache from earlier ones): the packed
-  // splits wait after their q tables, the window's at their end.
+  // Every launch starts as the one before it ends, and waits for it before it
+  // touches memory.  kPdlAll (its list comes from the launch before it, its q and
+  // cache from earlier ones): the packed splits wait after their q tables, the
+  // window's at their end.
   const bool wait_late = a.pdl == kPdlAll && z < p.splits;
   if (!wait_late) {
     grid_dependency_wait();
-    if (!a.next_late) grid_launch_dependents();
+    if (a.release == kReleaseAtOnce) grid_launch_dependents();
   }
   if (z >= p.splits) return;
   const bool packed = s >= p.tail_splits;
@@ -890,10 +888,7 @@ __global__ void __launch_bounds__(128, attn_ctas_per_sm(BITS, NB))
     const int c0 = packed ? p.t_tail : p.t_tail + s * kTailTok;
     window_tokens<BITS, MODE>(cv, a, p, *reinterpret_cast<WinSmem<BITS>*>(smem_raw), unit, gid, b, j0, nh, c0,
                               packed ? p.l : min(p.l, c0 + kTailTok), st);
-    if (wait_late && !packed) {
-      grid_dependency_wait();
-      if (!a.next_late) grid_launch_dependents();
-    }
+    if (wait_late && !packed) grid_dependency_wait();
     if (g < nh) {
       const float inv = only ? 1.0f / st.l : 1.0f;
       const long pidx = (gid * a.scfg.max_splits + s) * kNH + g;
@@ -920,7 +915,7 @@ __global__ void __launch_bounds__(128, attn_ctas_per_sm(BITS, NB))
       }
     }
   }
-  if (a.next_late) grid_launch_dependents();
+  if (a.release == kReleaseLate) grid_launch_dependents();
   const int blocks = (p.l + kGroup - 1) / kGroup;
   if (only) {
     if (MODE == kAttnMass && a.fold) {
@@ -1019,7 +1014,9 @@ cudaError_t launch_block_bits(const CacheView& cv, AttnArgs a, const SeqLens& le
   const int units = cv.H * a.nhc;
   const long ctas = (long)units * cv.B * a.splits, places = (long)attn_ctas_per_sm(BITS, NB) * kTargetSMs;
   a.window_last = ctas > places;
-  a.next_late = 2 * ctas > places;
+  // (the weights' launch: at once where there are places for it too, else once a
+  // CTA has its partial)
+  a.release = MODE != kAttnMass || a.fold ? kReleaseNever : 2 * ctas > places ? kReleaseLate : kReleaseAtOnce;
   // (the opt-in as in launch_bits: the same on every call)
   for (int n = 0; n <= kMaxOutliers; ++n) {
     size_t sz = 0;

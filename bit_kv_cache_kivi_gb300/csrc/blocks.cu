@@ -75,7 +75,7 @@ __device__ __forceinline__ float4 load_q4(const void* q, long head, int dt, bool
 
 template <int BITS>
 __global__ void __launch_bounds__(32 * kScoreWarps)
-    score_kernel(CacheView cv, const void* q, int q_dtype, int q_wide, int grp, float* scores, int row,
+    score_kernel(CacheView cv, const void* q, int q_dtype, int q_wide, int grp, float* scores, int row, int release,
                  const SeqLens lens) {
   constexpr float L = (float)((1 << BITS) - 1);
   // the B fragments of a round's heads, four a block: [block][zeros, scales][16-byte chunk group][lane]
@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(32 * kScoreWarps)
   const uint8_t* tiles = tile_at<BITS>(cv, unit, 0);
   float* out = scores + unit * row;
   grid_dependency_wait();
-  grid_launch_dependents();
+  if (release) grid_launch_dependents();
   // q of the first round before the tiles (the tables are made while those load)
   float4 q4[2];
   auto load_heads = [&](int j0) {
@@ -432,7 +432,7 @@ __global__ void __launch_bounds__(NT) select_kernel(CacheView cv, SelectArgs a, 
   const int n = a.step > 0 ? evict_left(nb, a.n, a.step) : min(a.n, nb);
   int* out = a.out + unit * a.out_row;
   grid_dependency_wait();
-  grid_launch_dependents();
+  if (a.release) grid_launch_dependents();
   select_unit<NT, K>(sm, a.scores + unit * a.row, nb, n, a.first, a.last, out);
   for (int i = n + threadIdx.x; i < a.out_row; i += NT) out[i] = -1;
   if (a.sums == nullptr) return;
@@ -579,7 +579,6 @@ __global__ void __launch_bounds__(kMassThreads) mass_kernel(CacheView cv, MassAr
   const int grp = a.Hq / cv.H, nhc = (grp + kHeadChunk - 1) / kHeadChunk;
   const int i = blockIdx.x * kMassThreads + threadIdx.x;
   grid_dependency_wait();
-  grid_launch_dependents();
   if (i >= a.row) return;
   const float before = a.mass_in ? a.decay * a.mass_in[unit * a.row + i] : 0.0f;
   float w = 0.0f;
@@ -608,9 +607,12 @@ __global__ void __launch_bounds__(kMassThreads) mass_kernel(CacheView cv, MassAr
 
 }  // namespace
 
-// Every launch here may start while the one before it on the stream ends; it
-// waits for it (grid_dependency_wait) before it touches memory, and lets the
-// next one start only then -- or, where it writes the cache, at its exit.
+// Every launch here may start as the one before it on the stream ends; it
+// waits for it (grid_dependency_wait) before it touches memory.  It lets the
+// next one start at its exit, or, where `release` says that the next one is
+// another kernel of the same call (which waits too), right after its own wait:
+// an attention call with the overlap on reads its q and its cache without
+// waiting, and the last launch of any other call has to be complete by then.
 template <typename... P, typename... A>
 cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t st, A... args) {
   cudaLaunchConfig_t lc = {};
@@ -626,7 +628,7 @@ cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, cudaStrea
 }
 
 cudaError_t launch_block_scores(const CacheView& cv, const void* q, int q_dtype, int Hq, float* scores, int row,
-                                const SeqLens& lens, cudaStream_t st) {
+                                bool release, const SeqLens& lens, cudaStream_t st) {
   // four CTAs an SM (their loads in flight are 128 KB): one wave, or a CTA a unit
   const long wave = 4l * kTargetSMs / ((long)cv.H * cv.B);
   const int need = (row + kScoreTiles - 1) / kScoreTiles;
@@ -636,7 +638,8 @@ cudaError_t launch_block_scores(const CacheView& cv, const void* q, int q_dtype,
   if (cv.bits == 3) kernel = score_kernel<3>;
   if (cv.bits == 4) kernel = score_kernel<4>;
   const int wide = ((uintptr_t)q & 15u) == 0;
-  return launch_early(kernel, grid, 32 * kScoreWarps, st, cv, q, q_dtype, wide, Hq / cv.H, scores, row, lens);
+  return launch_early(kernel, grid, 32 * kScoreWarps, st, cv, q, q_dtype, wide, Hq / cv.H, scores, row, (int)release,
+                      lens);
 }
 
 cudaError_t launch_select(const CacheView& cv, const SelectArgs& a, int most, const SeqLens& lens, cudaStream_t st) {

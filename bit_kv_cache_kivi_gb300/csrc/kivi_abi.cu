@@ -847,8 +847,8 @@ KIVI_API kivi_status kivi_block_scores(kivi_cache* c, const void* q, kivi_dtype 
   if (!device_accessible(q, dev) || !device_accessible(scores, dev)) return KIVI_EINVAL;
   kivi::SeqLens sl;
   seq_lens(c, &sl);
-  return cuda_status(kivi::launch_block_scores(view(c), q, (int)q_dtype, c->cfg.n_q_heads, scores, n_blocks, sl,
-                                               static_cast<cudaStream_t>(stream)));
+  return cuda_status(kivi::launch_block_scores(view(c), q, (int)q_dtype, c->cfg.n_q_heads, scores, n_blocks,
+                                               false, sl, static_cast<cudaStream_t>(stream)));
 }
 
 KIVI_API kivi_status kivi_select_blocks(kivi_cache* c, const float* scores, int n_blocks, int n_select, int keep_first,
@@ -905,9 +905,10 @@ KIVI_API kivi_status kivi_decode_attention_topk(kivi_cache* c, const void* q, ki
   const kivi::CacheView cv = view(c);
   // (the attention builds its q tables while the selection runs)
   kivi_status s = cuda_status(
-      kivi::launch_block_scores(cv, q, (int)q_dtype, c->cfg.n_q_heads, scores, n_blocks, sl, st));
+      kivi::launch_block_scores(cv, q, (int)q_dtype, c->cfg.n_q_heads, scores, n_blocks, true, sl, st));
   if (s != KIVI_OK) return s;
-  const kivi::SelectArgs sel = select_args(scores, n_blocks, n_select, keep_first, keep_last, blocks);
+  kivi::SelectArgs sel = select_args(scores, n_blocks, n_select, keep_first, keep_last, blocks);
+  sel.release = 1;
   s = cuda_status(kivi::launch_select(cv, sel, most_blocks(c), sl, st));
   if (s != KIVI_OK) return s;
   return list_attention(c, q, q_dtype, blocks, n_select, out, softmax_scale, workspace, st, kivi::kPdlAll);
@@ -1022,6 +1023,7 @@ KIVI_API kivi_status kivi_evict_blocks(kivi_cache* c, kivi_cache* into, const fl
   seq_lens(c, &sl);
   kivi::SelectArgs a = select_args(mass, n_blocks, n_keep, keep_first, keep_last, kept);
   a.step = evict_step(c);
+  a.release = 1;  // (the copies follow)
   a.out_row = kept_row;
   a.sums = mass_out;
   a.sums_row = mass_out_blocks;

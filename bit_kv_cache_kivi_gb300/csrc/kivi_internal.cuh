@@ -385,8 +385,8 @@ struct AttnArgs {
   // ordinary launch.
   int pdl;
   // The block attention: the order of its splits, and when the next launch may
-  // start (see block_attn_kernel)
-  int window_last, next_late;
+  // start (see block_attn_kernel; kReleaseNever but for the weights' launch)
+  int window_last, release;
   // kAttnList: tiles (packed blocks) of every unit, [unit][list_stride], of
   // which a sequence takes the first min(list_len, its packed blocks)
   const int* list;
@@ -415,6 +415,8 @@ struct AttnArgs {
 enum : int { kAttnAll = 0, kAttnList = 1, kAttnMass = 2, kAttnListOne = 3 };
 __host__ __device__ constexpr bool attn_listed(int mode) { return mode == kAttnList || mode == kAttnListOne; }
 __host__ __device__ constexpr bool attn_pairs(int mode) { return mode == kAttnList || mode == kAttnMass; }
+
+enum : int { kReleaseNever = 0, kReleaseAtOnce = 1, kReleaseLate = 2 };
 
 // kPdlOverlap: launched after other work on the stream that writes neither
 // q nor the cache (for instance another attention call): the CTAs read the
@@ -454,8 +456,9 @@ __host__ __device__ __forceinline__ int evict_left(int nb, int n_keep, int step)
 }
 
 // Upper bounds of q.k over every packed block into scores [B][H][row].
+// release: the next launch is another kernel of the same call.
 cudaError_t launch_block_scores(const CacheView& cv, const void* q, int q_dtype, int Hq, float* scores, int row,
-                                const SeqLens& lens, cudaStream_t st);
+                                bool release, const SeqLens& lens, cudaStream_t st);
 
 struct SelectArgs {
   const float* scores;  // [B][H][row]
@@ -469,6 +472,7 @@ struct SelectArgs {
   // window's blocks behind them, then zeros: [B][H][sums_row]; may be `scores`
   float* sums;
   int sums_row;
+  int release;  // the next launch is another kernel of the same call
 };
 // most: the most blocks of any sequence.
 cudaError_t launch_select(const CacheView& cv, const SelectArgs& a, int most, const SeqLens& lens, cudaStream_t st);

@@ -356,8 +356,10 @@ kivi_status kivi_set_attention_overlap(kivi_cache *c, int enable);
  * head), contiguous, 4-byte aligned, in device or page-locked host memory as
  * every per-call buffer, of at most 2^26 entries a row (KIVI_ESHAPE).
  * Every kernel is launched as a programmatic dependent of the one before it on
- * the stream: it starts while that one ends and waits for it before it touches
- * memory, so the stream's order holds. */
+ * the stream: it starts as that one ends and waits for it before it touches
+ * memory, so the stream's order holds.  A call lets no launch after it start
+ * before it has completed, so an overlapping attention call
+ * (kivi_set_attention_overlap) may read what it wrote. */
 
 /* Whole packed blocks of sequence b: floor(nq_v(l) / G); -1 if c is NULL or b
  * is no sequence.  Host only. */

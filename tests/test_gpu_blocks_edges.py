@@ -37,3 +37,57 @@ def test_long_windows(R, policy, grp, bits, tiles):
                 per = np.zeros(mass.shape[2])
                 np.add.at(per, np.arange(p.lengths[b]) // G, w.sum(0))
                 assert np.allclose(mass[b, h], per, rtol=1e-4, atol=1e-6)  # (bounds: test_attention_mass)
+
+
+@pytest.mark.parametrize("op", ["blocks", "topk", "mass", "mass of long rows"])
+def test_an_overlapping_call_reads_what_a_block_operator_wrote(op):
+    """The output of a block operator as the queries of an overlapping attention call, and the block operator's own
+    queries as that call's output: the last launch that is not an overlapping call has completed by then."""
+    from bit_kv_cache_kivi_gb300.kivi import KiviCache
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    l = 3000 if op == "mass" else 60000
+
+    def make(n):
+        c = KiviCache(batch=1, n_kv_heads=2, n_q_heads=8, max_tokens=-(-n // 32) * 32)
+        k, v = (torch.randn((1, 2, n, 128), generator=gen, device="cuda", dtype=torch.float16) for _ in range(2))
+        c.prefill(k, v)
+        return c
+    a, b = make(l), make(200)
+    b.set_splits(3)  # (the plan does not change with the setting)
+    blocks = torch.arange(a.packed_blocks(), dtype=torch.int32, device="cuda").expand(1, 2, -1).contiguous()
+    mass = torch.zeros((1, 2, a.cfg.max_tokens // G), device="cuda")
+    x, y = (torch.empty((1, 8, 128), dtype=torch.float16, device="cuda") for _ in range(2))
+
+    def run(overlap):
+        b.set_overlap(overlap)
+        got = []
+        for seed in range(20):
+            q = torch.randn((1, 8, 128), generator=torch.Generator(device="cuda").manual_seed(seed), device="cuda").half() * 4
+            x.fill_(7.0)
+            if op == "blocks":
+                a.attention_blocks(q, blocks, out=x)
+            elif op == "topk":
+                a.attention_topk(q, 1500, out=x)
+            else:
+                a.attention_mass(q, mass, out=x)
+            if not overlap:
+                torch.cuda.synchronize()
+            b.attention(x, out=y)
+            got += [x.clone(), y.clone()]
+            # ... and a call that replaces the queries of the one before it
+            if op == "blocks":
+                a.attention_blocks(q, blocks, out=x)
+            elif op == "topk":
+                a.attention_topk(q, 1500, out=x)
+            else:
+                a.attention_mass(q, mass, out=x)
+            if not overlap:
+                torch.cuda.synchronize()
+            b.attention(y, out=q)
+            got += [x.clone(), q]
+        torch.cuda.synchronize()
+        b.set_overlap(False)
+        return got
+    want = run(False)
+    for u, v in zip(want, run(True)):
+        assert torch.equal(u, v)

@@ -404,7 +404,8 @@ kivi_status kivi_select_blocks(kivi_cache *c, const float *scores, int n_blocks,
 /* kivi_decode_attention over the listed blocks and the window only:
  * blocks[B][H][n_list].  Sequence b reads the first min(n_list,
  * kivi_packed_blocks(c, b)) entries of its rows, in any order; an entry that
- * is no block of the sequence is skipped, a block listed twice counts twice.
+ * is no block of the sequence is skipped (nothing that any block holds counts
+ * in its place), a block listed twice counts twice.
  * n_list = 0 (blocks may be NULL) attends over the window alone.  q, out,
  * softmax_scale and the errors are those of kivi_decode_attention; the
  * workspace has kivi_block_workspace_bytes.  The overlap setting is ignored,

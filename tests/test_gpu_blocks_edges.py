@@ -91,3 +91,31 @@ def test_an_overlapping_call_reads_what_a_block_operator_wrote(op):
     want = run(False)
     for u, v in zip(want, run(True)):
         assert torch.equal(u, v)
+
+
+@pytest.mark.parametrize("bits,grp,outliers,qtype", [(2, 4, 0, "f16"), (4, 7, 0, "bf16"), (8, 8, 2, "f32"), (3, 2, 1, "f16"),
+                                                     (8, 4, 0, "f16"), (2, 7, 0, "f32")])
+def test_entries_that_name_no_block_read_nothing(bits, grp, outliers, qtype):
+    """Block 0 full of NaN and infinities, which no list names: holes anywhere in the list, first and last in a warp's share."""
+    p = Pair(B=2, H=2, T_=900, bits=bits, grp=grp, outliers=outliers, qtype=qtype, seed=6)
+    c, nb = p.cache, p.blocks(0)
+    lists = np.full((2, 2, nb), -1, np.int32)
+    rng = np.random.default_rng(4)
+    for b in range(2):
+        for h in range(2):
+            at = rng.permutation(nb)[:11]
+            lists[b, h, at] = rng.permutation(np.arange(1, nb))[:11]
+    lists[1, 0, 1:9] = [nb, 2**31 - 1, -2**31, nb + 7, -1, -1, nb, -1]
+    tiles = c.state_views()["tiles"]
+    tiles[:, :, 0] = torch.tensor([0x00, 0x7e, 0xff, 0x7f, 0x00, 0x7c, 0x00, 0xfc], dtype=torch.uint8,
+                                  device="cuda").repeat(tiles.shape[3] // 8 + 1)[:tiles.shape[3]]
+    dev = torch.from_numpy(lists).cuda()
+    for splits in (0, 2, 7):
+        c.set_splits(splits)
+        out = T.out_float(c.attention_blocks(p.q, dev)).reshape(2, 2, grp, 128)
+        for b in range(2):
+            for h in range(2):
+                row = lists[b, h]
+                row = row[(row >= 0) & (row < nb)].astype(np.int64)
+                tokens = np.concatenate([(row[:, None] * G + np.arange(G)).reshape(-1), np.arange(nb * G, 900)])
+                assert err(out[b, h], p.attend(b, h, tokens)[1], qtype) <= T.ATTN_TOL

@@ -680,6 +680,12 @@ int most_blocks(const kivi_cache* c) { return kivi::packed_blocks(max_len(c), c-
 
 bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
 
+// Rows of n and m 4-byte entries per (batch, KV head) that share memory.
+bool rows_overlap(const kivi_cache* c, const void* p, int n, const void* q, int m) {
+  const uintptr_t units = (uintptr_t)c->cfg.batch * c->cfg.n_kv_heads;
+  return p && q && (uintptr_t)p < (uintptr_t)q + 4 * units * m && (uintptr_t)q < (uintptr_t)p + 4 * units * n;
+}
+
 // Entries of a row at most (as many blocks as int tokens make): the kernels
 // count them in int.
 constexpr int kMaxRow = 1 << 26;
@@ -797,6 +803,7 @@ kivi_status select_checks(const kivi_cache* c, const float* scores, int n_blocks
   if (n_select < 1 || n_select > kMaxRow) return KIVI_ESHAPE;
   if (keep_first < 0 || keep_last < 0 || (long)keep_first + keep_last > n_select) return KIVI_ESHAPE;
   if (!scores || !blocks || !aligned4(scores) || !aligned4(blocks)) return KIVI_EINVAL;
+  if (rows_overlap(c, scores, n_blocks, blocks, n_select)) return KIVI_EINVAL;
   return KIVI_OK;
 }
 
@@ -934,6 +941,7 @@ KIVI_API kivi_status kivi_decode_attention_mass(kivi_cache* c, const void* q, ki
   if (!(decay >= 0.0f && decay <= 1.0f)) return KIVI_EINVAL;
   if (n_blocks > kMaxRow || n_blocks < (max_len(c) + c->cfg.group - 1) / c->cfg.group) return KIVI_ESHAPE;
   if (!records || !aligned16(records) || records_bytes < kivi_block_records_bytes(c)) return KIVI_EWORKSPACE;
+  if (mass_in != mass_out && rows_overlap(c, mass_in, n_blocks, mass_out, n_blocks)) return KIVI_EINVAL;
   int dev = 0;
   const kivi_status ds = launch_device(c, &dev);
   if (ds != KIVI_OK) return ds;
@@ -999,6 +1007,9 @@ KIVI_API kivi_status kivi_evict_blocks(kivi_cache* c, kivi_cache* into, const fl
   if (kept_row > 0 && (!kept || !aligned4(kept))) return KIVI_EINVAL;
   if (mass_out && (!aligned4(mass_out) || (mass_out == mass && mass_out_blocks != n_blocks))) return KIVI_EINVAL;
   if (mass_out && mass_out_blocks < most_out) return KIVI_ESHAPE;
+  if (rows_overlap(c, kept, kept_row, mass, n_blocks) || rows_overlap(c, kept, kept_row, mass_out, mass_out_blocks) ||
+      (mass_out != mass && rows_overlap(c, mass_out, mass_out_blocks, mass, n_blocks)))
+    return KIVI_EINVAL;
   // two handles on the same memory, or on parts of it
   if (into != c) {
     size_t n[3], m[3];

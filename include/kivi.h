@@ -354,7 +354,9 @@ kivi_status kivi_set_attention_overlap(kivi_cache *c, int enable);
  * The calls work on each KV head by itself, and take the query heads that
  * share it together.  Their float and int arrays are rows per (batch, KV
  * head), contiguous, 4-byte aligned, in device or page-locked host memory as
- * every per-call buffer, of at most 2^26 entries a row (KIVI_ESHAPE).
+ * every per-call buffer, of at most 2^26 entries a row (KIVI_ESHAPE).  Those
+ * of a call do not overlap (KIVI_EINVAL), but that a result may take its
+ * source's place whole where a call says so.
  * Every kernel is launched as a programmatic dependent of the one before it on
  * the stream: it starts as that one ends and waits for it before it touches
  * memory, so the stream's order holds.  A call lets no launch after it start

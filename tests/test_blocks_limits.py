@@ -24,3 +24,37 @@ def test_longer_windows_are_refused(K):
         assert lib.kivi_decode_attention_blocks(h, P, 1, P, 4, P, 0.0, P, ws, None) == K.KIVI_ESHAPE
         assert lib.kivi_decode_attention_topk(h, P, 1, 4, 0, 0, P, 4092, P, P, 0.0, P, ws, None) == K.KIVI_ESHAPE
         assert lib.kivi_decode_attention_mass(h, P, 1, P, 0.0, P, P, 4092, 1.0, P, ws, P, rec, None) == K.KIVI_ESHAPE
+
+
+def test_rows_that_overlap_are_refused(K):
+    """A result may take its source's place whole; any other overlap would have
+    one unit's rows written while another's are read."""
+    lib = K.lib()
+    with Handle(K, length=4000) as h, Handle(K, base=1 << 34) as into:  # 2 x 4 units, 124 blocks
+        Q = 1 << 28
+        ws, rec = K.kivi_block_workspace_bytes(h), K.kivi_block_records_bytes(h)
+        bytes_of = lambda n: 4 * 8 * n  # noqa: E731
+        free = lib.kivi_select_blocks(h, Q, 124, 4, 0, 0, 2 * Q, None)  # what a call gets that passes every check
+        inside = (0, 4, bytes_of(124) - 4)
+        for at in inside:
+            assert lib.kivi_select_blocks(h, Q, 124, 4, 0, 0, Q + at, None) == K.KIVI_EINVAL
+            assert lib.kivi_decode_attention_topk(h, P, 1, 4, 0, 0, Q, 124, Q + at, P, 0.0, P, ws, None) == K.KIVI_EINVAL
+        assert lib.kivi_select_blocks(h, Q, 124, 4, 0, 0, Q + bytes_of(124), None) == free
+        assert lib.kivi_select_blocks(h, Q, 124, 4, 0, 0, Q - bytes_of(4), None) == free
+        assert lib.kivi_select_blocks(h, Q, 124, 4, 0, 0, Q - bytes_of(4) + 4, None) == K.KIVI_EINVAL
+
+        def mass(a, b):
+            return lib.kivi_decode_attention_mass(h, P, 1, P, 0.0, a, b, 125, 1.0, P, ws, P, rec, None)
+        for a, b in ((Q, Q + 4), (Q + 4, Q), (Q, Q + bytes_of(125) - 4), (Q + 4 * 125, Q)):
+            assert mass(a, b) == K.KIVI_EINVAL
+        assert mass(Q, Q) == mass(Q, Q + bytes_of(125)) == mass(None, Q) == free
+
+        def evict(m, kept, out, to=into, out_row=125):
+            return lib.kivi_evict_blocks(h, to, m, 125, 20, 0, 0, kept, 20, out, out_row, None)
+        for to in (into, h):
+            for m, kept, out in ((Q, Q, None), (Q, Q + bytes_of(125) - 4, 2 * Q), (Q, 2 * Q, 2 * Q + 4 * 20), (Q, 2 * Q, Q + 4),
+                                 (Q + 4 * 125, 2 * Q, Q)):
+                assert evict(m, kept, out, to) == K.KIVI_EINVAL
+            assert evict(Q, 2 * Q, Q, to) == evict(Q, 2 * Q, 3 * Q, to) == evict(Q, 2 * Q, None, to) == free
+            assert evict(Q, Q + bytes_of(125), Q + bytes_of(125 + 20), to) == free
+        assert K.kivi_cache_length(h) == 4000 and K.kivi_cache_length(into) == 0

@@ -5,6 +5,7 @@
 #include <math.h>
 #include <stdlib.h>
 
+#include <initializer_list>
 #include <mutex>
 
 #include "../../include/kivi.h"
@@ -23,6 +24,7 @@ struct kivi_cache {
   const void* ws_ready;     // workspace whose counter area is known to be zero
   const void* block_ready;  // the same of the block attention's workspace
   int device;               // the buffers' device (kNoDevice until the first launching call)
+  kivi_cache *prev, *next;  // every handle, see use_workspace
 };
 
 namespace {
@@ -36,6 +38,26 @@ kivi_status cuda_status(cudaError_t e) {
 }
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+
+// Every handle, so that one which takes up a workspace lets the others that
+// knew its counters to be zero forget it: its partials may lie where theirs
+// are counted, and they zero them again.  (A call on the workspace that its
+// handle knows takes no lock.)
+std::mutex g_handles_mu;
+kivi_cache* g_handles;
+
+bool workspace_ready(const void* const& ready, const void* workspace) {
+  return __atomic_load_n(&ready, __ATOMIC_RELAXED) == workspace;
+}
+
+// `mine` (ws_ready or block_ready of a handle) and no other becomes `workspace`.
+void use_workspace(const void*& mine, const void* workspace) {
+  std::lock_guard<std::mutex> lock(g_handles_mu);
+  for (kivi_cache* h = g_handles; h; h = h->next)
+    for (const void** ready : {&h->ws_ready, &h->block_ready})
+      if (*ready == workspace) __atomic_store_n(ready, nullptr, __ATOMIC_RELAXED);
+  __atomic_store_n(&mine, workspace, __ATOMIC_RELAXED);
+}
 
 constexpr int kNoDevice = -1;   // not yet known
 constexpr int kAnyDevice = -2;  // managed buffers: reachable from every device
@@ -317,6 +339,12 @@ KIVI_API kivi_status kivi_cache_init(const kivi_config* cfg, const kivi_buffers*
   c->buf = *bufs;
   c->uniform = 1;
   c->device = kNoDevice;
+  {
+    std::lock_guard<std::mutex> lock(g_handles_mu);
+    c->next = g_handles;
+    if (g_handles) g_handles->prev = c;
+    g_handles = c;
+  }
   *out = c;
   return KIVI_OK;
 }
@@ -553,12 +581,12 @@ KIVI_API kivi_status kivi_decode_attention(kivi_cache* c, const void* q, kivi_dt
   if (ds != KIVI_OK) return ds;
   if (!device_accessible(q, dev) || !device_accessible(out, dev)) return KIVI_EINVAL;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (c->ws_ready != workspace) {
+  if (!workspace_ready(c->ws_ready, workspace)) {
     if (!device_accessible(workspace, dev)) return KIVI_EWORKSPACE;
     const WsLayout w = ws_layout(c->cfg);
     kivi_status z = cuda_status(cudaMemsetAsync(a.counters, 0, w.total - w.cnt_off, st));
     if (z != KIVI_OK) return z;
-    c->ws_ready = workspace;
+    use_workspace(c->ws_ready, workspace);
   }
   if (c->overlap) a.pdl = kivi::kPdlOverlap;
   a.epoch_on = 1;  // every call on the cache's workspace keeps its generations
@@ -589,14 +617,14 @@ KIVI_API kivi_status kivi_decode_step(kivi_cache* c, const void* k_new, const vo
       !device_accessible(out, dev))
     return KIVI_EINVAL;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (c->ws_ready != workspace) {
+  if (!workspace_ready(c->ws_ready, workspace)) {
     if (!device_accessible(workspace, dev)) return KIVI_EWORKSPACE;
     // before the append, so that the attention's only predecessor is the append
     const WsLayout w = ws_layout(c->cfg);
     kivi_status z =
         cuda_status(cudaMemsetAsync(static_cast<char*>(workspace) + w.cnt_off, 0, w.total - w.cnt_off, st));
     if (z != KIVI_OK) return z;
-    c->ws_ready = workspace;
+    use_workspace(c->ws_ready, workspace);
   }
   // the append lets the attention start at once (its prologue, and the
   // packed splits on most steps, run beside the append)
@@ -636,6 +664,12 @@ KIVI_API kivi_status kivi_cache_reset(kivi_cache* c) {
 
 KIVI_API void kivi_cache_destroy(kivi_cache* c) {
   if (!c) return;
+  {
+    std::lock_guard<std::mutex> lock(g_handles_mu);
+    if (c->prev) c->prev->next = c->next;
+    else g_handles = c->next;
+    if (c->next) c->next->prev = c->prev;
+  }
   free(c->lens);
   free(c);
 }
@@ -744,14 +778,14 @@ kivi_status attention_checks(kivi_cache* c, const void* q, kivi_dtype q_dtype, c
 // Zeroes the counter area of a workspace that the handle has not seen last.  A
 // captured call zeroes it when it is replayed, so the handle has not seen it.
 kivi_status ready_workspace(kivi_cache* c, void* workspace, int dev, cudaStream_t st) {
-  if (c->block_ready == workspace) return KIVI_OK;
+  if (workspace_ready(c->block_ready, workspace)) return KIVI_OK;
   if (!device_accessible(workspace, dev)) return KIVI_EWORKSPACE;
   cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
   kivi_status z = cuda_status(cudaStreamIsCapturing(st, &capture));
   if (z != KIVI_OK) return z;
   const WsLayout w = ws_layout_of(c->cfg, block_max_splits(c->cfg));
   z = cuda_status(cudaMemsetAsync(static_cast<char*>(workspace) + w.cnt_off, 0, w.total - w.cnt_off, st));
-  if (z == KIVI_OK && capture == cudaStreamCaptureStatusNone) c->block_ready = workspace;
+  if (z == KIVI_OK && capture == cudaStreamCaptureStatusNone) use_workspace(c->block_ready, workspace);
   return z;
 }
 

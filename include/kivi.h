@@ -257,6 +257,9 @@ size_t kivi_attention_workspace_bytes(const kivi_cache *c);
  * given workspace pointer zeroes it (one cudaMemsetAsync on the stream) and
  * every call leaves it zero.  Do not write to the workspace between calls,
  * and do not share one workspace between calls that may overlap on the GPU.
+ * (Handles may use one in turn: each zeroes it when it takes it up again.
+ * Replays of a graph are not seen: a workspace that one was captured on serves
+ * no other handle.)
  * Each sequence attends over its own length; KIVI_ESTATE when a sequence is
  * empty. */
 kivi_status kivi_decode_attention(kivi_cache *c, const void *q,
@@ -372,8 +375,9 @@ int kivi_packed_blocks(const kivi_cache *c, int b);
  * kivi_attention_workspace_bytes.  A counter area is carried between calls, as
  * there: the first call that sees a workspace zeroes it (a call that is captured
  * into a graph before that, at every replay), do not write to it between calls
- * or share it between calls or graphs that may overlap on the GPU.  The
- * workspace of kivi_decode_attention is another one.  Host only. */
+ * or share it between calls or graphs that may overlap on the GPU; handles may
+ * use one in turn, as there.  The workspace of kivi_decode_attention is another
+ * one.  Host only. */
 size_t kivi_block_workspace_bytes(const kivi_cache *c);
 
 /* An upper bound of q.k over every block, from the block's key scales and

@@ -119,3 +119,38 @@ def test_entries_that_name_no_block_read_nothing(bits, grp, outliers, qtype):
                 row = row[(row >= 0) & (row < nb)].astype(np.int64)
                 tokens = np.concatenate([(row[:, None] * G + np.arange(G)).reshape(-1), np.arange(nb * G, 900)])
                 assert err(out[b, h], p.attend(b, h, tokens)[1], qtype) <= T.ATTN_TOL
+
+
+def test_handles_of_other_shapes_use_one_workspace_in_turn():
+    """Their counters lie elsewhere: each zeroes its own when it takes the workspace up again."""
+    from bit_kv_cache_kivi_gb300 import kivi
+    ps = [Pair(B=1, H=2, T_=3000, seed=1), Pair(B=3, H=2, T_=1400, grp=7, bits=4, seed=2), Pair(B=2, H=2, T_=2000, R=64, seed=3)]
+    n = max(max(kivi.kivi_block_workspace_bytes(p.cache.handle), kivi.kivi_attention_workspace_bytes(p.cache.handle)) for p in ps)
+    ws = torch.full((n,), 0x55, dtype=torch.uint8, device="cuda")
+    lists = [torch.arange(p.blocks(0), dtype=torch.int32, device="cuda").expand(p.B, p.H, -1).contiguous() for p in ps]
+    want = [(p.cache.attention_blocks(p.q, l), p.cache.attention_mass(p.q, torch.zeros(p.B, p.H, 94, device="cuda")),
+             p.cache.attention(p.q)) for p, l in zip(ps, lists)]
+    for turn in range(4):
+        for p, l, w in zip(ps, lists, want):
+            h, rec = p.cache.handle, p.cache._records
+            for _ in range(2):
+                got = [torch.full_like(p.q, float("nan")) for _ in w]
+                kivi.kivi_decode_attention_blocks(h, p.q, kivi.KIVI_F16, l, l.shape[2], got[0], 0.0, ws, n)
+                kivi.kivi_decode_attention_mass(h, p.q, kivi.KIVI_F16, got[1], 0.0, None, torch.zeros(p.B, p.H, 94, device="cuda"),
+                                                94, 1.0, ws, n, rec, rec.numel())
+                assert torch.equal(got[0], w[0]) and torch.equal(got[1], w[1])
+                if turn % 2:  # (the whole-cache attention's own layout)
+                    kivi.kivi_decode_attention(h, p.q, kivi.KIVI_F16, got[2], 0.0, ws, n)
+                    assert torch.equal(got[2], w[2])
+
+
+def test_a_handle_that_is_gone_leaves_no_trace():
+    """Handles come and go beside one that keeps its workspace."""
+    p = Pair(T_=1000)
+    blocks = torch.arange(20, dtype=torch.int32, device="cuda").expand(2, 2, 20).contiguous()
+    want = p.cache.attention_blocks(p.q, blocks)
+    others = [Pair(T_=300 + 50 * i) for i in range(4)]
+    for i in (1, 3, 0, 2):
+        others[i].cache.attention_blocks(others[i].q, blocks)
+        others[i] = None
+        assert torch.equal(p.cache.attention_blocks(p.q, blocks), want)

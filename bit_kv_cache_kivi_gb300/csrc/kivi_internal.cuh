@@ -116,9 +116,13 @@ __host__ __device__ inline int block_split_tiles(const SplitCfg& sc, int tail_sp
                                                  bool* fused) {
   int per = (tiles + 3) / 4 * 4, best = 0x7fffffff;
   *fused = false;
-  // one place a unit: short lists and the window in one CTA (360 4-bit units of
-  // 7 heads: 8 tiles 15.7 us for 18.6, 24 tiles 25.5 for 26.4)
-  if (sc.budget == 1 && tail_splits == 1 && tiles <= 16) {
+  // one place a unit, or so many units that a round more or less of them counts
+  // little: short lists and the window in one CTA (360 4-bit units of 7 heads: 8
+  // tiles 15.7 us for 18.6, 24 tiles 25.5 for 26.4; 1216 2-bit units, 8 tiles:
+  // 32.0 for 39.5, 512 8-bit units, 1.7 rounds, 25.3 for 30.7; but 609 2-bit units
+  // of 16 tiles, a CTA more than places, 29.6 for 27.7)
+  const bool one = sc.budget == 1 || 2l * sc.units >= 3l * sc.per_sm * kTargetSMs;
+  if (one && tail_splits == 1 && tiles <= 16) {
     *fused = true;
     return per;
   }

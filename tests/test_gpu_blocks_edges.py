@@ -184,3 +184,31 @@ def test_f32_outputs_tell_a_pair_from_one_weight(bits, policy, R, grp, outliers)
                     one = (w / w.max(1, keepdims=True)).astype(np.float16).astype(np.float64)
                     lost = (one / one.sum(1, keepdims=True)) @ p.kv(b, h)[1][at]
                     assert T.attn_err(lost, ref) > 2 * F32_TOL
+
+
+@pytest.mark.parametrize("B,H,grp,bits,n,one", [(152, 8, 4, 2, 8, True), (87, 7, 4, 2, 8, False), (64, 8, 2, 8, 5, True),
+                                                (86, 8, 7, 4, 9, True), (1500, 1, 1, 3, 1, True)])
+def test_short_lists_of_very_many_units(B, H, grp, bits, n, one):
+    """More units than CTAs run at once: list and window in one CTA a unit, which writes no partials, from one and a half
+    rounds of them on."""
+    from bit_kv_cache_kivi_gb300 import kivi
+    T_ = 330
+    p = Pair(B=2, H=H, T_=T_, bits=bits, grp=grp, lengths=[T_, 41], seed=n)
+    lists = np.stack([[random_list(np.random.default_rng(h), p.blocks(b), n, "some") for h in range(H)] for b in range(2)])
+    c = kivi.KiviCache(batch=B, n_kv_heads=H, n_q_heads=H * grp, max_tokens=352, bits=bits)
+    rep = lambda x: x.repeat(B // 2 + 1, *[1] * (x.dim() - 1))[:B].contiguous()  # noqa: E731
+    c.prefill(rep(T.dev(p.wl.k, "f16")), rep(T.dev(p.wl.v, "f16")), ([T_, 41] * B)[:B] if B <= 1024 else None)
+    size = kivi.kivi_block_workspace_bytes(c.handle)
+    ws = torch.full((size,), 0x55, dtype=torch.uint8, device="cuda")
+    q, out = rep(p.q), torch.full((B, H * grp, 128), float("nan"), device="cuda", dtype=torch.float16)
+    kivi.kivi_decode_attention_blocks(c.handle, q, kivi.KIVI_F16, rep(torch.from_numpy(lists).cuda()), n, out, 0.0, ws, size)
+    if B <= 1024:  # (else the two sequences are of one length, and differ from p's second)
+        assert torch.equal(out, rep(out[:2]))
+    got = T.out_float(out[:2].contiguous()).reshape(2, H, grp, 128)
+    for b in range(2 if B <= 1024 else 1):
+        for h in range(H):
+            row = lists[b, h][lists[b, h] >= 0].astype(np.int64)
+            tokens = np.concatenate([(row[:, None] * G + np.arange(G)).reshape(-1), np.arange(p.blocks(b) * G, p.lengths[b])])
+            assert err(got[b, h], p.attend(b, h, tokens)[1], "f16") <= T.ATTN_TOL
+    partials = B * H * 8 * 128 * 4  # the first split's outputs of every unit, and more behind them
+    assert bool((ws[:partials] == 0x55).all()) == one

@@ -603,7 +603,7 @@ __device__ __forceinline__ void packed_blocks_split(const CacheView& cv, const A
   for (int i = 0; i < 4; ++i) Z[i] = 0.0f;
   uint32_t pb[2][2], pl[2][2];  // the weights of the tile before (see softmax_p)
   float ts[NB];
-  int sk = warp, sp = 0;  // the stages of tiles k and k - 1 (S >= kWarps)
+  int sk = warp, sp = 0;  // the stages of tiles k and k - 1 (S > kWarps)
   int turn = 0, tp = 0;   // ... and their turns there
   bool failed = false;
 #pragma unroll 1
@@ -1000,13 +1000,28 @@ __global__ void __launch_bounds__(128, attn_ctas_per_sm(BITS, NB))
 
 // Stages of a CTA's ring: as many as attn_ctas_per_sm CTAs per SM leave room
 // for, and its dynamic shared memory.
+constexpr size_t ring_stride(int bits, int n_out) {
+  return (size_t)(2 * kGroup * (kHeadDim * bits / 8) + 8 * kHeadDim - kStageOff + outlier_block_bytes(n_out));
+}
+template <int NB>
+constexpr size_t ring_fixed(int n_out) {
+  return sizeof(BlockState<NB>) + (n_out > 0 ? (size_t)kNH * kHeadDim * 4 : 0) + 16;
+}
+template <int BITS, int NB>
+constexpr int ring_room(int n_out) {
+  const size_t per_cta = (size_t)228 * 1024 / attn_ctas_per_sm(BITS, NB) - 1024 - 512;
+  return (int)((per_cta - ring_fixed<NB>(n_out)) / ring_stride(BITS, n_out));
+}
 template <int BITS, int NB>
 int ring_stages(int n_out, size_t* smem) {
-  const size_t stride = kTileBytes<BITS> - kStageOff + (size_t)outlier_block_bytes(n_out);
-  const size_t per_cta = (size_t)228 * 1024 / attn_ctas_per_sm(BITS, NB) - 1024 - 512;
-  const size_t fixed = sizeof(BlockState<NB>) + (n_out > 0 ? (size_t)kNH * kHeadDim * 4 : 0) + 16;
-  int S = (int)((per_cta - fixed) / stride);
-  S = S < kWarps ? kWarps : (S > kRingMax ? kRingMax : S);
+  static_assert(ring_stride(BITS, 0) == kTileBytes<BITS> - kStageOff, "a stage is a tile but for its key zeros");
+  // (with kWarps stages a warp's tile would wait for the copy that only the end
+  // of its tile before, in the same stage, lets go out)
+  static_assert(ring_room<BITS, NB>(0) > kWarps && ring_room<BITS, NB>(1) > kWarps && ring_room<BITS, NB>(2) > kWarps &&
+                    ring_room<BITS, NB>(3) > kWarps && ring_room<BITS, NB>(kMaxOutliers) > kWarps,
+                "a stage more than warps");
+  const size_t stride = ring_stride(BITS, n_out), fixed = ring_fixed<NB>(n_out);
+  const int S = ring_room<BITS, NB>(n_out) < kRingMax ? ring_room<BITS, NB>(n_out) : kRingMax;
   const size_t packed = (S * stride + 15) / 16 * 16 + fixed;
   *smem = packed > sizeof(WinSmem<BITS>) ? packed : sizeof(WinSmem<BITS>);
   return S;

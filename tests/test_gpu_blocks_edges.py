@@ -212,3 +212,144 @@ def test_short_lists_of_very_many_units(B, H, grp, bits, n, one):
             assert err(got[b, h], p.attend(b, h, tokens)[1], "f16") <= T.ATTN_TOL
     partials = B * H * 8 * 128 * 4  # the first split's outputs of every unit, and more behind them
     assert bool((ws[:partials] == 0x55).all()) == one
+
+
+# ------------------------------------------------------------------ long rows, many units
+
+@pytest.mark.parametrize("B,H,grp,bits,blocks,outliers,qtype", [
+    (16, 4, 4, 2, 1000, 0, "f16"), (16, 4, 7, 4, 1000, 0, "bf16"), (8, 8, 18, 8, 1000, 0, "f32"), (16, 4, 9, 3, 515, 2, "f16"),
+    (1, 8, 4, 2, 6001, 0, "f16"), (16, 40, 3, 2, 130, 1, "f16")])
+def test_scores_of_many_groups(B, H, grp, bits, blocks, outliers, qtype):
+    """Rows of more groups of 64 blocks than CTAs share them: tables of q used again for the next group, or made again
+    where the heads take several rounds."""
+    from bit_kv_cache_kivi_gb300.kivi import KiviCache, key_scale_pos
+    l, L = blocks * G + 32 + 9, 2 ** bits - 1
+    gen = torch.Generator(device="cuda").manual_seed(blocks + grp)
+    c = KiviCache(batch=B, n_kv_heads=H, n_q_heads=H * grp, max_tokens=-(-l // 32) * 32, bits=bits, outliers=outliers)
+    lengths = [l] + [int(x) for x in np.random.default_rng(1).integers(l // 3, l, B - 1)]
+    k = torch.randn((B, H, l, 128), generator=gen, device="cuda", dtype=torch.float16)
+    k[:, :, :, 5] *= 4
+    c.prefill(k, k, lengths)
+    q = torch.randn((B, H * grp, 128), generator=gen, device="cuda").to({"f16": torch.float16, "bf16": torch.bfloat16,
+                                                                        "f32": torch.float32}[qtype])
+    del k
+    n = blocks + 70
+    out = torch.full((B, H, n), float("nan"), device="cuda")
+    c.block_scores(q, out=out)
+    lv = c.layout_views()
+    at = torch.tensor([key_scale_pos(ch, bits) for ch in range(128)], device="cuda")
+    ref = torch.full((B, H, blocks), -float("inf"), dtype=torch.float64, device="cuda")
+    tol = torch.zeros_like(ref)
+    for b in range(B):
+        nb = c.packed_blocks(b)
+        z, s = (lv[x][b, :, :nb, at].view(torch.float16).double() for x in ("zero_k", "scale_k"))
+        qb = q[b].double().view(H, grp, 128)
+        qmax = qb.abs().amax(2)
+        for j in range(grp):
+            x = qb[:, j, None, :]
+            value = torch.maximum(x * z, x * (z + L * s)).sum(2)
+            size = ((x * z).abs() + L * (x * s).abs()).sum(2)
+            if outliers:
+                idx = lv["outl_idx"][b, :, :nb, :outliers].long()
+                val = lv["outl_val"][b, :, :nb].contiguous().view(torch.float16).double()
+                prod = torch.gather(x.expand(H, nb, 128), 2, idx)[:, :, None] * val
+                value += prod.sum(3).amax(2)
+                size += prod.abs().sum(3).amax(2)
+            ref[b, :, :nb] = torch.maximum(ref[b, :, :nb], value)
+            # (the bound of test_scores)
+            t = (2.0 ** -16 + 2.0 ** -22) * size + 2.0 ** -24 * qmax[:, j, None] * size.amax(1, keepdim=True)
+            tol[b, :, :nb] = torch.maximum(tol[b, :, :nb], t)
+        assert torch.all(out[b, :, nb:] == -float("inf"))
+        assert torch.all((out[b, :, :nb].double() - ref[b, :, :nb]).abs() <= tol[b, :, :nb])
+
+
+@pytest.mark.parametrize("place", ["in place", "into", "into, over the masses"])
+@pytest.mark.parametrize("bits,policy,R,outliers,blocks,keep,first,last,kind", [
+    (2, 0, 32, 0, 513, 200, 1, 2, "normal"), (3, 1, 64, 2, 600, 599, 0, 0, "ties"), (4, 0, 128, 0, 1100, 37, 4, 8, "ties"),
+    (8, 1, 32, 0, 1025, 1000, 0, 9, "odd"), (2, 0, 64, 4, 4200, 2100, 2, 3, "normal"), (2, 0, 32, 0, 4097, 4095, 0, 0, "equal"),
+    (4, 0, 32, 0, 4096, 0, 0, 0, "narrow")])
+def test_evictions_of_long_rows(place, bits, policy, R, outliers, blocks, keep, first, last, kind):
+    """Past the rows that one launch evicts: every selection of more than 512 blocks, and the copies behind it."""
+    from bit_kv_cache_kivi_gb300.kivi import KiviCache
+    from test_gpu_blocks import live_tiles, rough, select_ref
+    B, H = 3, 2
+    lengths = [blocks * G + R + 7, (blocks * 2 // 3) * G + R, 5]
+    new_cache = lambda n: KiviCache(batch=B, n_kv_heads=H, n_q_heads=H, max_tokens=-(-n // R) * R, bits=bits, residual=R,  # noqa: E731
+                                    policy=policy, outliers=outliers)
+    c = new_cache(max(lengths))
+    gen = torch.Generator(device="cuda").manual_seed(keep)
+    for x in c.buffers.values():
+        x.copy_(torch.randint(0, 256, x.shape, generator=gen, device="cuda", dtype=torch.uint8))
+    c.set_lengths(lengths)
+    before = {n: x.clone() for n, x in c.state_views().items()}
+    nb, left = [c.packed_blocks(b) for b in range(B)], [c.evict_left(keep, b) for b in range(B)]
+    assert nb[0] == blocks
+    new = [lengths[b] - G * (nb[b] - left[b]) for b in range(B)]
+    row = -(-max(lengths) // G) + 1
+    mn = rough(np.random.default_rng(blocks), (B, H, row), kind)
+    mass = torch.from_numpy(mn).cuda()
+    out_row, to = row, c
+    if place != "in place":
+        to = new_cache(max(new))
+        to.buffers["tiles"].fill_(0xA5)
+    if place == "into":
+        out_row = -(-max(new) // G) + 1
+        mass_out = torch.full((B, H, out_row), float("nan"), device="cuda")
+    else:
+        mass_out = mass
+    kept = c.evict_blocks(mass, keep, keep_first=first, keep_last=last, into=None if to is c else to, mass_out=mass_out)
+    kn, mo, after = kept.cpu().numpy(), mass_out.cpu().numpy(), to.state_views()
+    assert to.lengths == new and kn.shape == (B, H, max(left))
+    if to is not c:
+        assert c.lengths == lengths and all(torch.equal(c.state_views()[n], before[n]) for n in before)
+    for b in range(B):
+        tail = live_tiles(lengths[b], R, policy) - nb[b]
+        held = -(-lengths[b] // G) - nb[b]
+        for h in range(H):
+            want = select_ref(mn[b, h], nb[b], left[b], first, last)[:left[b]]
+            assert np.array_equal(kn[b, h], np.concatenate([want, np.full(max(left) - left[b], -1)]))
+            src = np.concatenate([want, np.arange(nb[b], nb[b] + tail)]).astype(int)
+            assert torch.equal(after["tiles"][b, h, :len(src)], before["tiles"][b, h][torch.from_numpy(src).cuda()])
+            if to is not c:
+                assert torch.all(after["tiles"][b, h, len(src):] == 0xA5)
+            elif left[b] < nb[b]:
+                assert torch.equal(after["tiles"][b, h, nb[b] + tail:], before["tiles"][b, h, nb[b] + tail:])
+            for ring in ("ring_k", "ring_v"):
+                assert torch.equal(after[ring][b, h], before[ring][b, h])
+            m = np.concatenate([mn[b, h][want], mn[b, h][nb[b]:nb[b] + held]])
+            assert np.array_equal(mo[b, h], np.concatenate([m, np.zeros(out_row - len(m), np.float32)]), equal_nan=True)
+
+
+def test_captured_with_overlapping_calls():
+    """Block operators and overlapping attention calls that read what they wrote, in one graph and replayed."""
+    a, b = Pair(B=1, H=2, T_=20000, grp=4, seed=1), Pair(B=1, H=2, T_=200, grp=4, seed=2)
+    blocks = torch.arange(a.blocks(0), dtype=torch.int32, device="cuda").expand(1, 2, -1).contiguous()
+    mass, new = torch.rand((1, 2, 640), device="cuda"), torch.empty((1, 2, 640), device="cuda")
+    q = a.q.clone()
+    outs = [torch.empty_like(q) for _ in range(7)]
+    b.cache.set_splits(3)  # (the plan does not change with the setting)
+
+    def calls(x, overlap):
+        b.cache.set_overlap(overlap)
+        a.cache.attention_blocks(q, blocks, out=x[0])
+        b.cache.attention(x[0], out=x[1])
+        b.cache.attention(x[0], out=x[2])
+        a.cache.attention_mass(x[1], mass, mass_out=new, out=x[3])
+        b.cache.attention(x[3], out=x[4])
+        a.cache.attention_topk(x[4], 400, out=x[5])
+        b.cache.attention(x[5], out=x[6])
+        b.cache.set_overlap(False)
+    calls(outs, False)  # (the scratch is made by the first calls)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        calls(outs, True)
+    for seed in range(6):
+        q.copy_(torch.randn(q.shape, generator=torch.Generator().manual_seed(seed)).half() * 4)
+        for x in outs:
+            x.fill_(7.0)
+        g.replay()
+        got = [x.clone() for x in outs + [new]]
+        want = [torch.empty_like(q) for _ in outs]
+        calls(want, False)
+        assert all(torch.equal(x, y) for x, y in zip(got, want + [new]))

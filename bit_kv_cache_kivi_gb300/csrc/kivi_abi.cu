@@ -514,13 +514,25 @@ KIVI_API int kivi_attention_splits(const kivi_cache* c, int l) {
 
 namespace {
 
+// Whether some sequence, n tokens longer, takes more splits than the two
+// levels of merges do (a window of more than 16384 tokens that nothing packed
+// lies behind, or an override beside one).
+bool too_many_splits(const kivi_cache* c, int n, bool overlapped) {
+  if (max_tail_splits(c->cfg) < kivi::kMaxSplits) return false;
+  for (int b = 0; b < (c->uniform ? 1 : c->cfg.batch); ++b)
+    if (plan_of(c, len_of(c, b) + n, overlapped).splits > kivi::kMaxSplits) return true;
+  return false;
+}
+
 // The attention launch arguments that depend on the lengths and the
-// workspace; KIVI_ESTATE when some sequence is empty.
+// workspace; KIVI_ESTATE when some sequence is empty, KIVI_ESHAPE for too many
+// splits.
 kivi_status attn_args(const kivi_cache* c, const void* q, kivi_dtype q_dtype, void* out, float softmax_scale,
                       char* ws, bool overlapped, kivi::AttnArgs* a, kivi::SeqLens* sl) {
   const int B = c->cfg.batch;
   for (int b = 0; b < (c->uniform ? 1 : B); ++b)
     if (len_of(c, b) <= 0) return KIVI_ESTATE;
+  if (too_many_splits(c, 0, overlapped)) return KIVI_ESHAPE;
   a->q = q;
   a->out = out;
   a->q_dtype = (int)q_dtype;
@@ -610,6 +622,7 @@ KIVI_API kivi_status kivi_decode_step(kivi_cache* c, const void* k_new, const vo
   if (!q || !out) return KIVI_EINVAL;
   if (!workspace || !aligned16(workspace) || ws_bytes < kivi_attention_workspace_bytes(c))
     return KIVI_EWORKSPACE;
+  if (too_many_splits(c, 1, false)) return KIVI_ESHAPE;
   int dev = 0;
   const kivi_status ds = launch_device(c, &dev);
   if (ds != KIVI_OK) return ds;
@@ -633,7 +646,7 @@ KIVI_API kivi_status kivi_decode_step(kivi_cache* c, const void* k_new, const vo
   kivi::AttnArgs a;
   kivi::SeqLens sl;
   kivi_status ast = attn_args(c, q, q_dtype, out, softmax_scale, static_cast<char*>(workspace), false, &a, &sl);
-  if (ast != KIVI_OK) return ast;  // not reached: every sequence holds a token now
+  if (ast != KIVI_OK) return ast;  // not reached: checked above, and every sequence holds a token now
   // Which tiles did the append write?  Under either policy, the only write
   // below t_tail = 32 floor(nq_v(l) / 32) is on a step where l - R reaches a
   // multiple of G: the value row leaving the window (Algorithm 1) or the
@@ -1152,6 +1165,7 @@ KIVI_API kivi_status kivi_decode_attention_static(kivi_cache* c, const void* q,
   if (!device_accessible(q, dev) || !device_accessible(out, dev)) return KIVI_EINVAL;
   for (int b = 0; b < (c->uniform ? 1 : c->cfg.batch); ++b)
     if (len_of(c, b) <= 0) return KIVI_ESTATE;
+  if (too_many_splits(c, 0, false)) return KIVI_ESHAPE;
   void* ws = nullptr;
   kivi_status st = cuda_status(static_ws_address(&ws));
   if (st != KIVI_OK) return st;

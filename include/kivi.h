@@ -261,7 +261,9 @@ size_t kivi_attention_workspace_bytes(const kivi_cache *c);
  * Replays of a graph are not seen: a workspace that one was captured on serves
  * no other handle.)
  * Each sequence attends over its own length; KIVI_ESTATE when a sequence is
- * empty. */
+ * empty, KIVI_ESHAPE when one takes more than 256 splits, which is more than
+ * two levels of merges do (more than 16384 tokens in a window with nothing packed
+ * behind it, or an override of the splits beside such a window). */
 kivi_status kivi_decode_attention(kivi_cache *c, const void *q,
                                   kivi_dtype q_dtype, void *out,
                                   float softmax_scale, void *workspace,

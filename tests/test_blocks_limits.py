@@ -58,3 +58,22 @@ def test_rows_that_overlap_are_refused(K):
             assert evict(Q, 2 * Q, Q, to) == evict(Q, 2 * Q, 3 * Q, to) == evict(Q, 2 * Q, None, to) == free
             assert evict(Q, Q + bytes_of(125), Q + bytes_of(125 + 20), to) == free
         assert K.kivi_cache_length(h) == 4000 and K.kivi_cache_length(into) == 0
+
+
+def test_whole_attention_over_too_many_splits_is_refused(K):
+    """The whole-cache attention merges 256 splits: a window of 64 tokens a
+    split without a packed tile behind it has no other plan."""
+    lib, R = K.lib(), 32768
+    for length, refused in ((16384, False), (16385, True), (30000, True), (R + 31, True), (2 * R + 40, False)):
+        with Handle(K, residual=R, max_tokens=4 * R, length=length) as h:
+            assert (K.kivi_attention_splits(h, length) > 256) == refused
+            ws = K.kivi_attention_workspace_bytes(h)
+            got = [lib.kivi_decode_attention(h, P, 1, P, 0.0, P, ws, None),
+                   lib.kivi_decode_step(h, P, P, 1, P, 1, P, 0.0, P, ws, None)]
+            # (16384 tokens: the step's token is one too many)
+            assert got[0] == K.KIVI_ESHAPE if refused else got[0] != K.KIVI_ESHAPE
+            assert got[1] == K.KIVI_ESHAPE if refused and length != R + 31 or length == 16384 else got[1] != K.KIVI_ESHAPE
+            assert K.kivi_cache_length(h) == length
+            K.kivi_set_attention_splits(h, 1000)
+            if K.kivi_attention_splits(h, length) > 256:
+                assert lib.kivi_decode_attention(h, P, 1, P, 0.0, P, ws, None) == K.KIVI_ESHAPE

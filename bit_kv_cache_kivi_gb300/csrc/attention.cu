@@ -6,13 +6,13 @@
 namespace kivi {
 namespace {
 
-// Diagnostics: one thread waits, with the bounded wait above, on phase 0 of
-// an mbarrier that nothing completes (no copy is issued, no thread arrives),
-// and records the timeout in *status as a packed split does in the
-// workspace status word.
 // The slot the epoch probe waits on: it stays 0, and the probe waits for 1.
 __device__ unsigned g_probe_epoch;
 
+// Diagnostics: one thread waits, with the bounded wait of the staged tiles, on
+// phase 0 of an mbarrier that nothing completes (no copy is issued, no thread
+// arrives), and records the timeout in *status as a packed split does in the
+// workspace status word; then the same for the epoch wait.
 __global__ void wait_probe_kernel(int* status) {
   __shared__ __align__(8) unsigned long long bar;
   if (threadIdx.x == 0) {

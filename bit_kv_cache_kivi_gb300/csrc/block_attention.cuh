@@ -790,11 +790,11 @@ __device__ __forceinline__ void merge_splits(const float* po, const float* pml, 
 // once come unit by unit, the window's first: grid (splits, H * head_chunks, B).
 // Of more, every unit's packed splits start before the windows, as the longer
 // ones (window_last): grid (H * head_chunks, B, splits).  128 units of 128 8-bit
-// tiles (384 CTAs for 304 places) take 32.5 us so, 37.6 unit by unit; 8 units of
-// 256 tiles 10.0 us so, 9.7 unit by unit.
+// tiles (384 CTAs for 304 places) take 33.2 us so, 37.1 unit by unit; 8 units of
+// 256 tiles 10.5 us so, 10.3 unit by unit.
 // The next launch starts when this one has completed (attention calls with the
-// overlap on read its output without waiting), but for the weights' launch of
-// the same call (mass_kernel).
+// overlap on read its output without waiting), the weights' launch of the same
+// call (mass_kernel) too: 49.0 us for 131k tokens, as if it were let in earlier.
 template <int BITS, int NB, int MODE>
 __global__ void __launch_bounds__(128, attn_ctas_per_sm(BITS, NB))
     block_attn_kernel(CacheView cv, AttnArgs a, const SeqLens lens) {
@@ -826,7 +826,6 @@ __global__ void __launch_bounds__(128, attn_ctas_per_sm(BITS, NB))
   const bool wait_late = a.pdl == kPdlAll && z < p.splits;
   if (!wait_late) {
     grid_dependency_wait();
-    if (a.release == kReleaseAtOnce) grid_launch_dependents();
   }
   if (z >= p.splits) return;
   const bool packed = s >= p.tail_splits;
@@ -923,7 +922,6 @@ __global__ void __launch_bounds__(128, attn_ctas_per_sm(BITS, NB))
       }
     }
   }
-  if (a.release == kReleaseLate) grid_launch_dependents();
   const int blocks = (p.l + kGroup - 1) / kGroup;
   if (only) {
     if (MODE == kAttnMass && a.fold) {
@@ -1037,9 +1035,6 @@ cudaError_t launch_block_bits(const CacheView& cv, AttnArgs a, const SeqLens& le
   const int units = cv.H * a.nhc;
   const long ctas = (long)units * cv.B * a.splits, places = (long)attn_ctas_per_sm(BITS, NB) * kTargetSMs;
   a.window_last = ctas > places;
-  // (the weights' launch: at once where there are places for it too, else once a
-  // CTA has its partial)
-  a.release = MODE != kAttnMass || a.fold ? kReleaseNever : 2 * ctas > places ? kReleaseLate : kReleaseAtOnce;
   // (the opt-in as in launch_bits: the same on every call)
   for (int n = 0; n <= kMaxOutliers; ++n) {
     size_t sz = 0;

@@ -22,8 +22,8 @@ __host__ __device__ constexpr int attn_key_blocks(int grp) { return (grp < kHead
 __host__ __device__ constexpr int attn_ctas_per_sm(int bits, int nb) {
   return bits == 8 ? 2 : (bits == 4 && nb == 2 ? 3 : 4);
 }
-constexpr int kFlatMerge = 64;     // ... by the block attention in one level (more: two)
 constexpr int kMergeGroup = 16;    // split partials merged by one CTA (two levels at most)
+constexpr int kFlatMerge = 64;     // the block attention merges up to this many in one level
 constexpr int kTailTok = 64;       // tail tokens per tail split
 constexpr int kMaxSplits = kMergeGroup * kMergeGroup;
 
@@ -105,21 +105,20 @@ struct SplitCfg {
 // 384 listed tiles: a packed CTA of t tiles beside k - 1 others takes
 // {4, 5, 7, 8}[k] t + 8 k (24 k with more than four heads), more than 32 splits
 // 24, windows that start late 60 and as much (90: more than 32 tokens) a round of
-// the SMs, a fused one 24.  At
-// 2 bits, 4 heads, in us: 64 tiles of 80 units 11.9 as 6 splits beside the
-// window's (560 CTAs), 13.7 as 4 (400), 14.7 as 2 (240); 256 tiles of 8 units
-// 9.7 as 16 (144 CTAs), 10.5 as 22 (192); 96 tiles of 160 units 23.2 as 3 whose
-// windows start late, 28.8 as 2; 24 tiles of 256 units with the window on the
-// second of two 16.2, 17.2 as 1 beside it, 24 of 208 units 14.8 as 2 beside it;
-// 24 tiles of 256 units with windows of 128 tokens 19.1 as 1, 22.2 as 2.
+// the SMs, a fused one 24.  Whole caches of thousands of tiles are planned by the
+// same costs.  At 2 bits, 4 heads, in us: 64 tiles of 80 units 13.4 as 6 splits
+// beside the window's (560 CTAs), 13.6 as 4 (400), 16.5 as 2 (240); 256 tiles of 8
+// units 10.2 as 16 (144 CTAs), 10.8 as 22 (192); 96 tiles of 160 units 26.7 as 3
+// whose windows start late, 29.3 as 2; 24 tiles of 256 units with the window on
+// the second of two 18.3, 20.3 as 1 beside it, 18.9 as 2; 24 of 208 units 17.0 as 1
+// beside it, 17.2 as 2.
 __host__ __device__ inline int block_split_tiles(const SplitCfg& sc, int tail_splits, int tail_tokens, int tiles,
                                                  bool* fused) {
   int per = (tiles + 3) / 4 * 4, best = 0x7fffffff;
   *fused = false;
   // one place a unit, or so many units that a round more or less of them counts
-  // little: short lists and the window in one CTA (360 4-bit units of 7 heads: 8
-  // tiles 15.7 us for 18.6, 24 tiles 25.5 for 26.4; 1216 2-bit units, 8 tiles:
-  // 32.0 for 39.5, 512 8-bit units, 1.7 rounds, 25.3 for 30.7; but 609 2-bit units
+  // little: short lists and the window in one CTA (360 4-bit units of 7 heads, 8
+  // tiles: 16.0 us for 18.4; 1216 2-bit units, 8 tiles: 32.0 for 39.5, 512 8-bit units, 1.7 rounds, 25.3 for 30.7; but 609 2-bit units
   // of 16 tiles, a CTA more than places, 29.6 for 27.7)
   const bool one = sc.budget == 1 || 2l * sc.units >= 3l * sc.per_sm * kTargetSMs;
   if (one && tail_splits == 1 && tiles <= 16) {
@@ -388,9 +387,8 @@ struct AttnArgs {
   // and only the tail's readers do.  kPdlOverlap: see below.  0: an
   // ordinary launch.
   int pdl;
-  // The block attention: the order of its splits, and when the next launch may
-  // start (see block_attn_kernel; kReleaseNever but for the weights' launch)
-  int window_last, release;
+  // The block attention: the order of its splits (see block_attn_kernel)
+  int window_last;
   // kAttnList: tiles (packed blocks) of every unit, [unit][list_stride], of
   // which a sequence takes the first min(list_len, its packed blocks)
   const int* list;
@@ -414,13 +412,11 @@ struct AttnArgs {
 
 // What the attention kernel covers: every packed tile and the tail; listed
 // packed tiles and the tail; as the first, with every block's softmax sums
-// recorded; listed tiles, with one fp16 weight a token as the first (outputs
-// in bf16 round at 2^-9, the weights at 2^-12).
+// recorded; listed tiles, with one fp16 weight a token as the first (outputs in
+// bf16 round by up to 2^-8 of themselves, the weights by up to 2^-11).
 enum : int { kAttnAll = 0, kAttnList = 1, kAttnMass = 2, kAttnListOne = 3 };
 __host__ __device__ constexpr bool attn_listed(int mode) { return mode == kAttnList || mode == kAttnListOne; }
 __host__ __device__ constexpr bool attn_pairs(int mode) { return mode == kAttnList || mode == kAttnMass; }
-
-enum : int { kReleaseNever = 0, kReleaseAtOnce = 1, kReleaseLate = 2 };
 
 // kPdlOverlap: launched after other work on the stream that writes neither
 // q nor the cache (for instance another attention call): the CTAs read the

@@ -44,7 +44,7 @@ __device__ __forceinline__ float warp_max(float v) {
 // KB) is in flight at once, four CTAs an SM.  131k tokens of 8 units at 2 bits
 // take 3.9 us (16.8 MB, 4.3 TB/s; one block row of 4097 tokens 2.3 us), 16
 // sequences of up to 32k tokens, 4 KV heads of seven query heads, at 4 bits
-// 7.5 us (24 MB).
+// 7.3 us (24 MB).
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(32 * kScoreWarps)
 // indices above the threshold and the first few equal to it.  Bound by the
 // latency of its few barriers: up to K keys a thread stay in registers (K = 0:
 // a row of any length is read again for every pass).  64 rows of 127 keys take
-// 2.6 us, 8 rows of 4092 6.0 us, of which an empty launch is about 2; 1024
+// 2.7 us, 8 rows of 4092 6.2 us, of which an empty launch is about 2; 1024
 // threads of four keys for the latter (512 of eight: 6.8), 256 of four up to
 // 1024 keys (beside an eviction 1.1 us less than 1024 threads).
 

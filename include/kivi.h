@@ -386,11 +386,17 @@ size_t kivi_block_workspace_bytes(const kivi_cache *c);
  * zeros alone: scores[B][H][n_blocks] gets
  *   max over the KV head's query heads of
  *   sum_c max(q_c zero_c, q_c (zero_c + (2^bits - 1) scale_c))
- * (unscaled: no softmax scale; summed in 32 bits, a bound up to their
- * rounding), and -infinity from the sequence's last block on.  fp16 outlier channels add the largest of their exact q.k over the
- * block's tokens.  A channel whose keys are all equal in a block has scale 1
- * (see quantizer), so its bound is loose: still an upper bound.  q: as
- * kivi_decode_attention.
+ * (unscaled: no softmax scale), and -infinity from the sequence's last block on.
+ * fp16 outlier channels add the largest of their exact q.k over the block's
+ * tokens.  It is a bound up to its rounding, which a caller who prunes by it
+ * allows for: q_c and (2^bits - 1) max(q_c, 0) enter as fp16 pairs (2^-22 of
+ * themselves, or 2^-25 of the head's largest |q| where that is more; the second
+ * 2^bits - 1 times as much), and the products are summed in 32 bits, with
+ * truncation (about 2.4e-7 off in all on the average, 2^-16 of the sum of the
+ * terms' magnitudes at most).  A head whose q holds a NaN counts for no block, a
+ * block whose scales or zeros hold one for no head: -infinity where none is left.
+ * A channel whose keys are all equal in a block has scale 1 (see quantizer), so
+ * its bound is loose: still an upper bound.  q: as kivi_decode_attention.
  * KIVI_ESHAPE when n_blocks is below 1 or some sequence has more blocks. */
 kivi_status kivi_block_scores(kivi_cache *c, const void *q, kivi_dtype q_dtype,
                               float *scores, int n_blocks, void *stream);
@@ -411,16 +417,18 @@ kivi_status kivi_select_blocks(kivi_cache *c, const float *scores, int n_blocks,
 
 /* kivi_decode_attention over the listed blocks and the window only:
  * blocks[B][H][n_list].  Sequence b reads the first min(n_list,
- * kivi_packed_blocks(c, b)) entries of its rows, in any order; an entry that
+ * kivi_packed_blocks(c, b)) entries of its rows, in any order (those that name
+ * no block are among them: a list with holes is read no further); an entry that
  * is no block of the sequence is skipped (nothing that any block holds counts
  * in its place), a block listed twice counts twice.
  * n_list = 0 (blocks may be NULL) attends over the window alone.  q, out,
  * softmax_scale and the errors are those of kivi_decode_attention; the
  * workspace has kivi_block_workspace_bytes.  The overlap setting is ignored,
  * kivi_set_attention_splits applies.  The softmax weights enter the value
- * product as fp16 pairs (one fp16 each for bf16 queries, whose outputs round
- * at 2^-9, and in kivi_decode_attention), so f32 queries get outputs close to
- * f32.  KIVI_ESHAPE when n_list is negative, and, as from the attention calls
+ * product as fp16 pairs, so f32 queries get outputs about 3e-6 of the largest
+ * off (5e-6 at 8 bits, 1e-5 over 131k tokens); one fp16 each, 2^-11 of itself
+ * off at most, for bf16 queries, whose outputs round by up to 2^-8 of themselves,
+ * and in kivi_decode_attention.  KIVI_ESHAPE when n_list is negative, and, as from the attention calls
  * below, when R is above 65440. */
 kivi_status kivi_decode_attention_blocks(kivi_cache *c, const void *q,
                                          kivi_dtype q_dtype, const int *blocks,

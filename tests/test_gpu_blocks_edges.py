@@ -353,3 +353,27 @@ def test_captured_with_overlapping_calls():
         want = [torch.empty_like(q) for _ in outs]
         calls(want, False)
         assert all(torch.equal(x, y) for x, y in zip(got, want + [new]))
+
+
+@pytest.mark.parametrize("grp,outliers", [(4, 0), (9, 2)])
+def test_scores_of_nan(grp, outliers):
+    """A head whose q holds a NaN counts for no block, a block whose scales hold one for no head."""
+    p = Pair(B=2, H=2, T_=400, grp=grp, outliers=outliers, qtype="f32", seed=3)
+    c, nb = p.cache, p.blocks(0)
+    q = p.q.clone()
+    first = c.block_scores(q, out=torch.empty((2, 2, nb), device="cuda"))
+    heads = q.view(2, 2, grp, 128)
+    heads[0, 0, 1, 17] = float("nan")
+    rest = heads.clone()
+    rest[0, 0, 1] = rest[0, 0, 0]  # (a head twice changes no maximum)
+    got = c.block_scores(q, out=torch.empty_like(first))
+    assert torch.equal(got, c.block_scores(rest.view(q.shape), out=torch.empty_like(first)))
+    heads[1, 1] = float("nan")
+    got = c.block_scores(q, out=torch.empty_like(first))
+    assert torch.all(got[1, 1] == -float("inf")) and torch.equal(got[1, 0], first[1, 0])
+    c.layout_views()["scale_k"][0, 1, 3, 40] = 0x7e00
+    got = c.block_scores(p.q, out=torch.empty_like(first))
+    assert got[0, 1, 3] == -float("inf")
+    keep = torch.ones_like(first, dtype=torch.bool)
+    keep[0, 1, 3] = False
+    assert torch.equal(got[keep], first[keep])

@@ -377,3 +377,35 @@ def test_scores_of_nan(grp, outliers):
     keep = torch.ones_like(first, dtype=torch.bool)
     keep[0, 1, 3] = False
     assert torch.equal(got[keep], first[keep])
+
+
+@pytest.mark.parametrize("bits,policy,R,grp,outliers", [(2, 0, 32, 4, 0), (4, 0, 128, 7, 0), (8, 1, 64, 4, 2), (3, 1, 32, 8, 0),
+                                                       (2, 0, 96, 18, 1)])
+def test_memory_behind_the_tokens_counts_for_nothing(bits, policy, R, grp, outliers):
+    """The cache's unused tiles and ring slots, scratch, records and outputs full of NaN or of zeros: the same results."""
+    from bit_kv_cache_kivi_gb300 import kivi
+    lengths = [611, 1, R + 31, 2 * R + 33]
+    wl = Pair(B=4, H=2, T_=611, R=R, bits=bits, policy=policy, grp=grp, outliers=outliers, lengths=lengths, seed=8).wl
+    got = []
+    for byte in (0x00, 0x7f, 0xff):
+        c = T.gpu_cache(wl, capacity=R * -(-704 // R), policy=policy, outliers=outliers)
+        for x in c.buffers.values():
+            x.fill_(byte)
+        c.prefill(T.dev(wl.k, "f16"), T.dev(wl.v, "f16"), lengths)
+        q = T.dev(wl.q, "f16")
+        rows = lambda n, dtype=torch.float32: torch.full((4, 2, 4 * n), byte, dtype=torch.uint8, device="cuda").view(dtype)  # noqa: E731
+        nws, nrec = kivi.kivi_block_workspace_bytes(c.handle), kivi.kivi_block_records_bytes(c.handle)
+        ws, rec = (torch.full((n,), byte, dtype=torch.uint8, device="cuda") for n in (nws, nrec))
+        scores, blocks, mass = rows(25), rows(6, torch.int32), rows(25)
+        o1, o2, o3 = (torch.full((q.numel() * 2,), byte, dtype=torch.uint8, device="cuda").view(torch.float16).view(q.shape) for _ in range(3))
+        h = c.handle
+        kivi.kivi_decode_attention_topk(h, q, kivi.KIVI_F16, 6, 1, 1, scores, 25, blocks, o1, 0.0, ws, nws)
+        lists = torch.tensor([3, 0, -1, 9, 2, 2], dtype=torch.int32, device="cuda").expand(4, 2, 6).contiguous()
+        kivi.kivi_decode_attention_blocks(h, q, kivi.KIVI_F16, lists, 6, o2, 0.0, ws, nws)
+        kivi.kivi_decode_attention_mass(h, q, kivi.KIVI_F16, o3, 0.0, None, mass, 25, 1.0, ws, nws, rec, nrec)
+        kept, left = rows(25, torch.int32), rows(25)
+        c.evict_blocks(mass, 3, kept=kept, mass_out=left)
+        got.append([scores, blocks, o1, o2, o3, mass, kept, left, c.attention(q)])
+    for other in got[1:]:
+        assert all(torch.equal(x, y) for x, y in zip(got[0], other))
+    assert all(bool(torch.isfinite(x).all()) for x in got[0][2:])
